@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["qlora_nf4.cu", "nf4_table.cpp"]
 HEADERS = ["adapter_mma.cuh", "common.cuh", "fp8_gemm.cuh", "fp8_layer.cuh", "fp8_quant.cuh", "fp8_skinny.cuh",
            "gemm_kernel.cuh", "lora_mma.cuh", "merge_kernel.cuh", "pipeline.cuh", "quant_kernels.cuh",
-           "skinny_kernel.cuh", "nf4_table.hpp"]
+           "skinny_kernel.cuh", "nf4_table.hpp", "workspace.hpp"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

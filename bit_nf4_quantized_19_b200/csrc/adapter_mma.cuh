@@ -77,7 +77,7 @@ struct AdapterParams {
   int64_t pitch;
   const uint8_t *keep;    // bit-packed keep mask of the activation [M, act_cols], or null
   int64_t act_cols;
-  // QUANT
+  // QUANT (codes of the call's workspace, on a 256-byte address; rows of a multiple of 128)
   uint8_t *q_codes, *q_scales;
   int64_t q_pitch;
   // projection, each may be null: fp32 [rows, ld]; bf16 hi|lo of s*value [rows, 2 half]
@@ -159,6 +159,7 @@ QDEV uint32_t mul_bf16x2(uint32_t a, uint32_t f) {
                                    *reinterpret_cast<const __nv_bfloat162 *>(&f));
   return *reinterpret_cast<const uint32_t *>(&p);
 }
+// (p on a 32-byte address)
 QDEV void st_global_v8(void *p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
                "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])

@@ -18,6 +18,7 @@
 #include "nf4_table.hpp"
 #include "quant_kernels.cuh"
 #include "skinny_kernel.cuh"
+#include "workspace.hpp"
 
 using namespace qlora;
 
@@ -211,21 +212,6 @@ bool make_map_2d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint6
              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-// ------------------------------------------------------------------ workspace
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-struct Workspace {
-  char *base;
-  size_t used;
-  size_t cap;
-  void *take(size_t bytes) {
-    const size_t off = align256(used);
-    if (off + bytes > cap) return nullptr;
-    used = off + bytes;
-    return base + off;
-  }
-};
 
 // ---- launch geometry of the rank-r contractions (lora_mma_kernel)
 constexpr int kLmMaxSplits = kLmClusterMax;
