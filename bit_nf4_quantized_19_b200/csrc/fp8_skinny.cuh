@@ -11,7 +11,8 @@
 //     a ring of kS8Stages; two CTAs fit an SM, 128 KB in flight.
 //   - The products run on mma.sync m16n8k16 f16: every e4m3 and e5m2 code is exact in f16 (one
 //     conversion for two codes), products accumulate in fp32 and each block's sum is scaled
-//     by 2^(eW + eX) as it is added.  The contraction index is permuted inside a block so
+//     by 2^(eW + eX) as it is added, in two factors of half the exponent each (see s8_factors).  The
+//     contraction index is permuted inside a block so
 //     that a lane takes 16 consecutive codes of its rows: step w of a 16-byte piece is its
 //     word w, codes 0, 1 and 2, 3 the fragment's two halves, for W and X alike.
 //   - The CTAs of XA fit beside two of these on an SM (72 and 40 registers, small chunks), so the
@@ -60,7 +61,7 @@ struct Skinny8Params {
 struct Skinny8Plan {
   int C, blocks, off_b, off_recv, off_xa, off_bar, smem;
 };
-// X in one stage: the codes of eight tokens, their f16 fragments, eight factors.
+// X in one stage: the codes of eight tokens, their f16 fragments, eight pairs of factors.
 constexpr int kS8XCodes = 1024, kS8XFrags = 2048;
 constexpr int kS8XBytes = kS8XCodes + kS8XFrags + 128;
 inline Skinny8Plan skinny8_plan(int M, int K, int r, int C) {
@@ -94,6 +95,18 @@ QDEV void f8_to_f16x2(uint32_t w, uint32_t &lo, uint32_t &hi) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(a));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(b));
   }
+}
+
+// 2^(eX + eW) as two powers of two that fp32 holds whatever the bytes are, each with half of the
+// exponent: a block's sum d is taken times the first and, as it is added, times the second.  d is 0
+// or 2^-25 to 2^32 in size, so either the first product is exact (halves of -101 to 95) or the
+// whole one is beyond fp32 in the same direction.  (The one factor 2^(eX + eW) is infinite past 127,
+// which turns 0 into NaN and loses what codes below 1 bring back, and 0 below -149, where d still
+// brings products back.)
+QDEV float2 s8_factors(uint32_t bx, uint32_t bw) {
+  if (bx == kF8NanScale || bw == kF8NanScale) return make_float2(f8_scale(kF8NanScale), 1.0f);
+  const uint32_t sum = bx + bw;
+  return make_float2(f8_scale(sum >> 1), f8_scale(sum - (sum >> 1)));
 }
 
 // XE5M2: format of X.
@@ -190,8 +203,8 @@ __global__ void __launch_bounds__(kS8RegThreads, 2)
     }
   } else if (warp >= 9) {
     // ------------------------------------------------------------ X
-    // lane (g, c) converts 16 codes of token g at columns 64 h + 16 c of a block; lane t < 8 makes the factor of token t times the weight block's, from bytes requested
-    // 2 kAhead blocks before.
+    // lane (g, c) converts 16 codes of token g at columns 64 h + 16 c of a block; lane t < 8 makes the
+    // factors of token t with the weight block's, from bytes requested 2 kAhead blocks before.
     // Warp 9 + j takes the blocks i with i mod 2 = j (the ring is even, so its slots are its own).
     constexpr int kAhead = 2;
     static_assert(kS8Stages % 2 == 0, "a ring slot belongs to one X warp");
@@ -213,7 +226,7 @@ __global__ void __launch_bounds__(kS8RegThreads, 2)
       for (int u = 0; u < kAhead; ++u) {
         const int i = i0 + 2 * u;
         if (!ok || i >= nb) continue;
-        const float f = f8_scale(fw[u]) * f8_scale(fx[u]);
+        const float2 f = s8_factors(fx[u], fw[u]);
         if (i + 2 * kAhead < nb) {
           fx[u] = __ldg(px + i + 2 * kAhead);
           fw[u] = __ldg(pw + i + 2 * kAhead);
@@ -234,7 +247,7 @@ __global__ void __launch_bounds__(kS8RegThreads, 2)
           st_shared_v4(dst + h * 1024, o[0], o[1], o[2], o[3]);
           st_shared_v4(dst + h * 1024 + 512, o[4], o[5], o[6], o[7]);
         }
-        if (lane < kS8MaxTokens) reinterpret_cast<float *>(sX + s * kS8XBytes + kS8XCodes + kS8XFrags)[lane] = f;
+        if (lane < kS8MaxTokens) reinterpret_cast<float2 *>(sX + s * kS8XBytes + kS8XCodes + kS8XFrags)[lane] = f;
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
         s += 2;
@@ -265,7 +278,7 @@ __global__ void __launch_bounds__(kS8RegThreads, 2)
         xv[h][0] = ld_shared_v4(xb + h * 1024);
         xv[h][1] = ld_shared_v4(xb + h * 1024 + 512);
       }
-      const float2 f = reinterpret_cast<const float2 *>(sX + s * kS8XBytes + kS8XCodes + kS8XFrags)[c];   // tokens 2c, 2c + 1
+      const float4 f = reinterpret_cast<const float4 *>(sX + s * kS8XBytes + kS8XCodes + kS8XFrags)[c];   // tokens 2c, 2c + 1
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
       float d[4] = {0.f, 0.f, 0.f, 0.f};
@@ -281,10 +294,10 @@ __global__ void __launch_bounds__(kS8RegThreads, 2)
           mma_16816_f16(d, a, (w & 1) ? q.z : q.x, (w & 1) ? q.w : q.y);
         }
       }
-      acc[0] = fmaf(d[0], f.x, acc[0]);
-      acc[1] = fmaf(d[1], f.y, acc[1]);
-      acc[2] = fmaf(d[2], f.x, acc[2]);
-      acc[3] = fmaf(d[3], f.y, acc[3]);
+      acc[0] = fmaf(d[0] * f.x, f.y, acc[0]);
+      acc[1] = fmaf(d[1] * f.z, f.w, acc[1]);
+      acc[2] = fmaf(d[2] * f.x, f.y, acc[2]);
+      acc[3] = fmaf(d[3] * f.z, f.w, acc[3]);
       if (++s == kS8Stages) { s = 0; ph ^= 1u; }
     }
     // push the partial rows to the rank that finishes them, [this rank][row][token], once the

@@ -71,3 +71,55 @@ def test_workspace_at_any_16_byte_start(q, M, N, K, r):
         torch.cuda.synchronize()
         assert same(want, got), start
     assert q.device_status() == (0, 0)
+
+
+# ------------------------------------------------------------------ factors far from one on both operands
+FORMS = [1, 8, 12, 100, 300]      # tokens: the few-token kernel, the weight on the MMA's rows, whole tiles
+
+
+@pytest.mark.parametrize("M", FORMS)
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_large_factors_on_both_operands(q, M, fmt):
+    """Two blocks meet whose factors' product passes 2^128.  Rows of W without a value there, and rows
+    whose product is still a bf16 value, are what the formula gives; only the row whose product
+    is past bf16 is infinite.  Every product and sum is exact but for the rounding to bf16."""
+    import torch
+    rng = np.random.default_rng(M)
+    N, K = 256, 512
+    X = rng.integers(-4, 5, (M, K)).astype(np.float64)
+    X[:, :128] = 0.0
+    X[:, 0], X[:, 1] = 2.0 ** 106, 2.0 ** 90      # the first sets the block's factor, 2^98 or 2^91
+    W = rng.integers(-4, 5, (N, K)).astype(np.float64)
+    W[:, :128] = 0.0                              # rows 128 ..: a block of zeros, factor 2^-127
+    W[5, 0] = 2.0 ** 48                           # sets its block's factor, 2^40
+    W[7:128, 1] = 2.0 ** 32
+    Xq, Wq = q.fp8_quantize(dev(X), fmt=fmt), q.fp8_quantize_weight(dev(W))
+    assert int(Xq.scales[0, 0]) + int(Wq.scales[0, 0]) - 254 == (138 if fmt == "e4m3" else 131)
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy((X @ W.T).astype(np.float32)).to(torch.bfloat16)
+    Y, _ = q.fp8_linear_fwd(Xq, Wq)
+    torch.cuda.synchronize()
+    assert q.device_status() == (0, 0)
+    assert torch.isinf(want[:, 5]).all() and torch.isfinite(want).sum() == M * (N - 1)
+    assert torch.equal(Y.cpu(), want)
+
+
+@pytest.mark.parametrize("M", FORMS)
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_small_factors_on_both_operands(q, M, fmt):
+    """Two blocks meet whose factors' product is below 2^-149, fp32's smallest, while the sum of their
+    codes' products brings it back: 1024 products of (FMAX 2^-a) (448 2^-75) are 1.5 2^-123 (e4m3) or
+    1.5 2^-126, normal bf16 values; in the other rows they come with a sign."""
+    import torch
+    N, K = 256, 1024
+    top, a = (448.0, 75) if fmt == "e4m3" else (57344.0, 85)
+    sign = np.where(np.arange(N) % 3 == 0, -1.0, 1.0)
+    X, W = np.full((M, K), top * 2.0 ** -a), np.full((N, K), 448.0 * 2.0 ** -75) * sign[:, None]
+    Xq, Wq = q.fp8_quantize(dev(X), fmt=fmt), q.fp8_quantize_weight(dev(W))
+    assert int(Xq.scales[0, 0]) + int(Wq.scales[0, 0]) - 254 == -75 - a
+    want = torch.from_numpy(X @ W.T).to(torch.bfloat16)
+    assert torch.equal(want.double(), torch.from_numpy(X @ W.T))
+    Y, _ = q.fp8_linear_fwd(Xq, Wq)
+    torch.cuda.synchronize()
+    assert q.device_status() == (0, 0)
+    assert torch.equal(Y.cpu(), want)
