@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
       for (int j = 0; j < 4; ++j) {
         const int64_t m = (GRAD ? static_cast<int64_t>(pr0 + i) * 128 : row0) + lane + 32 * j;
         const int64_t blk = GRAD ? (row0 >> 7) : pr0 + i;
-        b[j] = (i < npr && m < p.tokens) ? __ldg(p.scales + m * p.pitch + blk) : 127u;
+        b[j] = (i < npr && m < p.tokens) ? ld_global_u8(p.scales + m * p.pitch + blk) : 127u;
       }
     };
     uint32_t cur[4], nxt[4];
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
       const uint8_t *kp = p.keep + ((m0 * p.act_cols + static_cast<int64_t>(GRAD ? (row0 >> 7) : pr0 + team) * 128 + 64 * shalf) >> 3);
       const int64_t kp_step = GRAD ? 32 * p.act_cols : 32;
       auto keep_now = [&]() -> uint2 {
-        return m_left > 0 ? __ldg(reinterpret_cast<const uint2 *>(kp)) : make_uint2(~0u, ~0u);
+        return m_left > 0 ? ld_global_v2(kp) : make_uint2(~0u, ~0u);
       };
       uint2 kb = team < npr ? keep_now() : make_uint2(~0u, ~0u);
       int rs = team, s = 2 * team + sub;
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
         if (p.split_terms) {
           float x[4] = {0.f, 0.f, 0.f, 0.f};
           if (j < p.r) {
-            const float4 f = *reinterpret_cast<const float4 *>(p.split_in + static_cast<int64_t>(row) * p.ld + p.j0 + j);
+            const float4 f = ld_global_f4(p.split_in + static_cast<int64_t>(row) * p.ld + p.j0 + j);
             x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
           }
           uint2 t[3];

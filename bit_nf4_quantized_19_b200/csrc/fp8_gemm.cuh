@@ -468,19 +468,19 @@ __global__ void __launch_bounds__(kFgThreads, 1)
         for (int j = 0; j < 4; ++j) {
           const int m = (FEW ? 0 : w.m0 + half) + lane + 32 * j;
           a[j] = 0x7F7F7F7Fu;    // rows past the end hold zero codes; their factor is one
-          if (m < p.M) a[j] = __ldg(reinterpret_cast<const uint32_t *>(p.sa + static_cast<int64_t>(m) * p.sa_pitch + 4 * g));
+          if (m < p.M) a[j] = ld_global_u32(p.sa + static_cast<int64_t>(m) * p.sa_pitch + 4 * g);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (ob + h >= p.out_blocks) continue;
           if (!DX) {
-            b[h] = __ldg(reinterpret_cast<const uint32_t *>(p.sw + static_cast<int64_t>(ob + h) * p.sw_pitch + 4 * g));
+            b[h] = ld_global_u32(p.sw + static_cast<int64_t>(ob + h) * p.sw_pitch + 4 * g);
           } else {
             uint32_t x = 0u;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (4 * g + j < p.kb_main)
-                x |= static_cast<uint32_t>(__ldg(p.sw + static_cast<int64_t>(4 * g + j) * p.sw_pitch + ob + h)) << (8 * j);
+                x |= ld_global_u8(p.sw + static_cast<int64_t>(4 * g + j) * p.sw_pitch + ob + h) << (8 * j);
             b[h] = x;
           }
         }
@@ -516,15 +516,15 @@ __global__ void __launch_bounds__(kFgThreads, 1)
 }
 
 // Y = bf16(sum of the splits' fp32 partials, in order).  total is a multiple of 4.
-__global__ void __launch_bounds__(256) fp8_reduce_kernel(const float *__restrict__ part, int splits, int64_t total,
-                                                         uint16_t *__restrict__ out) {
+__global__ void __launch_bounds__(256) fp8_reduce_kernel(const float *part, int splits, int64_t total,
+                                                         uint16_t *out) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   pdl_trigger();
   pdl_wait();
   if (i >= total) return;
-  float4 v = *reinterpret_cast<const float4 *>(part + i);
+  float4 v = ld_global_f4(part + i);
   for (int s = 1; s < splits; ++s) {
-    const float4 f = *reinterpret_cast<const float4 *>(part + s * total + i);
+    const float4 f = ld_global_f4(part + s * total + i);
     v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
   }
   *reinterpret_cast<uint2 *>(out + i) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kF8Threads) fp8_quantize_kernel(const __grid_c
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       v[u][h] = make_uint4(0u, 0u, 0u, 0u);
-      if (blk < p.blocks && col[u] * kF8Block + sub * 8 + h * 64 < p.cols) v[u][h] = ld_global_nc_v4(src + h * 64);
+      if (blk < p.blocks && col[u] * kF8Block + sub * 8 + h * 64 < p.cols) v[u][h] = ld_global_v4(src + h * 64);
     }
   }
   bool bad = false;

@@ -190,12 +190,11 @@ __global__ void __launch_bounds__(kS8RegThreads, 2)
     pdl_wait();
     // (r is a multiple of 8: four values at a time, every part's load issued before the sum)
     const int n4 = (p.M * p.r) >> 2;
-    const float4 *src = reinterpret_cast<const float4 *>(p.xa);
 #pragma unroll 2
     for (int i = lane; i < n4; i += 32) {
       float4 pa[kS8MaxXaParts], v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int q = 0; q < kS8MaxXaParts; ++q) pa[q] = q < p.xa_parts ? src[q * n4 + i] : v;
+      for (int q = 0; q < kS8MaxXaParts; ++q) pa[q] = q < p.xa_parts ? ld_global_f4(p.xa + 4 * (q * n4 + i)) : v;
 #pragma unroll
       for (int q = 0; q < kS8MaxXaParts; ++q) { v.x += pa[q].x; v.y += pa[q].y; v.z += pa[q].z; v.w += pa[q].w; }
       reinterpret_cast<float4 *>(sXA)[i] = v;
@@ -215,8 +214,8 @@ __global__ void __launch_bounds__(kS8RegThreads, 2)
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int i = j0 + 2 * u;
-      fx[u] = i < nb ? __ldg(px + i) : 0u;
-      fw[u] = i < nb ? __ldg(pw + i) : 0u;
+      fx[u] = i < nb ? ld_global_u8(px + i) : 0u;
+      fw[u] = i < nb ? ld_global_u8(pw + i) : 0u;
     }
     int s = j0;
     uint32_t ph = 0;
@@ -228,8 +227,8 @@ __global__ void __launch_bounds__(kS8RegThreads, 2)
         if (!ok || i >= nb) continue;
         const float2 f = s8_factors(fx[u], fw[u]);
         if (i + 2 * kAhead < nb) {
-          fx[u] = __ldg(px + i + 2 * kAhead);
-          fw[u] = __ldg(pw + i + 2 * kAhead);
+          fx[u] = ld_global_u8(px + i + 2 * kAhead);
+          fw[u] = ld_global_u8(pw + i + 2 * kAhead);
         }
         // the slot's product warps are done with it: its copies were issued after they were
         ok = wait_bar_warp(&x_full[s], ph, wt);

@@ -47,6 +47,37 @@ QDEV bool elect_one() {
 QDEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 QDEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Loads behind a pdl_wait.  The kernel before may have written the words while this grid already
+// lived, which the non-coherent path (__ldg, const __restrict__) rules out; these are coherent and,
+// like the wait, volatile, so they stay behind it.
+QDEV uint32_t ld_global_u8(const uint8_t *p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+QDEV uint32_t ld_global_u32(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+QDEV uint2 ld_global_v2(const void *p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+// (streamed data; with the wider L2 fetch the quantizer takes what it did on the non-coherent path:
+// 8192 x 22016 90 us and 89, 8192 x 8192 35 and 37; without it 93 and 38)
+QDEV uint4 ld_global_v4(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+QDEV float4 ld_global_f4(const float *p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+
 // The two halves of a cluster barrier, for work between them.
 QDEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 QDEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }

@@ -33,6 +33,7 @@
 #pragma once
 #include "common.cuh"
 #include "fp8_quant.cuh"
+#include "pipeline.cuh"
 
 namespace qlora {
 
@@ -344,8 +345,8 @@ __global__ void __launch_bounds__(256, F8 ? 6 : 1) qlora_xa_kernel(const __grid_
       const int per_row = rows / 16;
       for (int u = tid; u < p.M * per_row; u += 256) {
         const int t = u / per_row, k = a0 + (u - t * per_row) * 16;
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p.codes + static_cast<int64_t>(t) * p.K + k));
-        const float f = f8_scale(__ldg(p.scales + static_cast<int64_t>(t) * p.pitch + (k >> 7)));
+        const uint4 w = ld_global_v4(p.codes + static_cast<int64_t>(t) * p.K + k);
+        const float f = f8_scale(ld_global_u8(p.scales + static_cast<int64_t>(t) * p.pitch + (k >> 7)));
         const uint4 lo = p.e5m2 ? f8_decode8<true>(make_uint2(w.x, w.y), f) : f8_decode8<false>(make_uint2(w.x, w.y), f);
         const uint4 hi = p.e5m2 ? f8_decode8<true>(make_uint2(w.z, w.w), f) : f8_decode8<false>(make_uint2(w.z, w.w), f);
         uint4 *dst = reinterpret_cast<uint4 *>(sX + t * xpitch + k - a0);
