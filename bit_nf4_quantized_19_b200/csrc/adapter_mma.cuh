@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kAmThreads, 1)
   uint64_t *raw_empty = raw_full + kAmMaxRaw;
   uint64_t *acc_full = raw_empty + kAmMaxRaw;
   uint64_t *acc_empty = acc_full + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+  uint64_t *drain = acc_empty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   int *abort_flag = reinterpret_cast<int *>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -227,6 +228,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
     }
     for (int i = 0; i < kAmMaxRaw; ++i) { mbar_init(&raw_full[i], 2); mbar_init(&raw_empty[i], 8); }
     for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 8); }
+    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -303,6 +305,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     bool ready = false;   // this stage's tile was seen complete while the last one was issued
+    bool issued = false;
     for (int i = 0; i < nst; ++i) {
       const bool first = (i & (kAmChain - 1)) == 0;
       const bool last = (i & (kAmChain - 1)) == kAmChain - 1 || i + 1 == nst;
@@ -321,8 +324,15 @@ __global__ void __launch_bounds__(kAmThreads, 1)
       }
       ad += slot_step;
       bd += slot_step;
+      issued = true;
       ready = __all_sync(0xffffffffu, peek) != 0;
       if (++s == p.n_op) { s = 0; ph ^= 1u; ad = ad0; bd = bd0; }
+    }
+    // every MMA issued has completed before the block gives up its shared memory and TMEM
+    // (bounded); unless a wait ran out, the last drain has seen the same
+    if (issued) {
+      if (el) mma_commit(drain);
+      wait_bar_warp(drain, 0, final_wt);
     }
     __syncwarp();
   } else if (warp == 2 && F8) {

@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       // peer's own copy of that stage has landed, or not at all after an abort: the
       // wait is bounded either way, and this CTA's copies have landed when it ends.
       volatile int no_abort = 0;
-      const Waiter final_wt{&no_abort, p.limit_ns};
+      const Waiter final_wt{&no_abort, drain_limit_ns(p.limit_ns)};
       for (int s = 0; s < kStages; ++s)
         if (armedB & (1u << s)) wait_bar(&full_B[s], (lastB >> s) & 1u, final_wt);
     }
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     if (lane == 0) {
       volatile int no_abort = 0;
-      const Waiter final_wt{&no_abort, p.limit_ns};
+      const Waiter final_wt{&no_abort, drain_limit_ns(p.limit_ns)};
       for (int s = 0; s < kStagesW; ++s)
         if (armedW & (1u << s)) wait_bar(&full_W[s], (lastW >> s) & 1u, final_wt);
     }
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       // released (bounded).
       commit(drain);
       volatile int no_abort = 0;
-      const Waiter final_wt{&no_abort, p.limit_ns};
+      const Waiter final_wt{&no_abort, drain_limit_ns(p.limit_ns)};
       wait_bar(drain, 0, final_wt);
     }
   } else if (warp == 1) {
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       // the leader's MMAs read this CTA's shared memory and write its TMEM: they
       // complete before either is released (bounded)
       volatile int no_abort = 0;
-      const Waiter final_wt{&no_abort, p.limit_ns};
+      const Waiter final_wt{&no_abort, drain_limit_ns(p.limit_ns)};
       wait_bar(drain, 0, final_wt);
     }
   } else if (warp >= 4 && warp < 8) {

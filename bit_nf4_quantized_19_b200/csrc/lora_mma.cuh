@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kLmThreads, 1)
       if (++s == S) { s = 0; ph ^= 1u; }
     }
     volatile int no_abort = 0;
-    const Waiter fw{&no_abort, p.limit_ns};
+    const Waiter fw{&no_abort, drain_limit_ns(p.limit_ns)};
     for (int k = 0; k < S; ++k)
       if (armed & (1u << k)) wait_bar(&full[k], (last >> k) & 1u, fw);
   } else if (warp == 1 && lane == 0) {
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kLmThreads, 1)
     const int q = warp & 3;
     const int rl = q * 32 + lane;
     volatile int no_abort = 0;
-    const Waiter dw{&no_abort, p.limit_ns};
+    const Waiter dw{&no_abort, drain_limit_ns(p.limit_ns)};
     const bool got = __all_sync(0xffffffffu, wait_bar(done, 0, dw) ? 1 : 0);
     tc_fence_after();
     const int pitch = lm_partial_pitch(p.nn);

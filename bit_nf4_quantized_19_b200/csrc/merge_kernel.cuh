@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
     }
     // no copy may still be in flight when the block exits
     volatile int no_abort = 0;
-    const Waiter fw{&no_abort, p.limit_ns};
+    const Waiter fw{&no_abort, drain_limit_ns(p.limit_ns)};
     for (int st = 0; st < p.stages; ++st) wait_bar(&full[st], 0, fw);
     wait_bar(base_full, 0, fw);
   } else if (warp == 1 && lane == 0) {
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
 #pragma unroll
     for (int i = 0; i < 16; ++i) L[i] = p.levels[i];
     volatile int no_abort = 0;
-    const Waiter dw{&no_abort, p.limit_ns};
+    const Waiter dw{&no_abort, drain_limit_ns(p.limit_ns)};
     const bool got = __all_sync(0xffffffffu, (wait_bar(done, 0, dw) && wait_bar(base_full, 0, dw)) ? 1 : 0) &&
                      *abort_flag == 0;
     tc_fence_after();

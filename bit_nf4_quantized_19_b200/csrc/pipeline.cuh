@@ -25,10 +25,6 @@ QDEV bool wait_bar_warp(uint64_t *bar, uint32_t parity, const Waiter &w) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, w) ? 1 : 0) != 0;
 }
 
-// Limit of the waits for what is already in flight (copies, MMAs) before a block gives up
-// its shared memory and TMEM: long enough whatever the caller's limit is.
-QDEV uint64_t drain_limit_ns(uint64_t limit_ns) { return limit_ns > 50000000ull ? limit_ns : 50000000ull; }
-
 // One lane of a converged warp.
 QDEV bool elect_one() {
   uint32_t r;

@@ -254,7 +254,15 @@ __global__ void __launch_bounds__(kQuantThreads, kQuantCtasPerSm) nf4_quantize_k
     __syncthreads();   // tables and barriers ready; the previous group's amax and wmax consumed
     uint4 v[kQuantPasses];
     if (whole(g)) {
-      if (!__syncthreads_and(wait_bar(&full[s], ph, waiter))) break;
+      if (!__syncthreads_and(wait_bar(&full[s], ph, waiter))) {
+        // given up: the copies of this and the next stages land before the block may end (bounded)
+        volatile int no_abort = 0;
+        const Waiter final_wt{&no_abort, drain_limit_ns(limit_ns)};
+        for (int k = 0; tid == 0 && k < kQuantStages; ++k)
+          if (g + k * G < ngroups && whole(g + k * G))
+            wait_bar(&full[(it + k) % kQuantStages], static_cast<uint32_t>((it + k) / kQuantStages) & 1u, final_wt);
+        break;
+      }
       const uint32_t src = smem_u32(ring + s * kQuantStageBytes) + static_cast<uint32_t>((bl * kBlock + sub * 8) * 2);
 #pragma unroll
       for (int p = 0; p < kQuantPasses; ++p)

@@ -225,6 +225,11 @@ __global__ void __launch_bounds__(kSkThreads, 3) qlora_skinny_kernel(
     }
   }
 
+  volatile int no_abort = 0;
+  const Waiter final_wt{&no_abort, drain_limit_ns(p.limit_ns)};
+  // given up: the boxes in flight land before the block may end (bounded)
+  for (int mb = 0; !ok && mb < nmb; ++mb) wait_bar(&bars[mb], 0, final_wt);
+
   // ---- 3. push the partial Y rows to the rank that finishes them: slot
   // [this rank][row within the owner's R][token] of the owner's receive buffer
   {
@@ -250,7 +255,8 @@ __global__ void __launch_bounds__(kSkThreads, 3) qlora_skinny_kernel(
   // XA comes from the XA kernel: wait for that grid (a no-op when launched plainly)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i = tid; i < p.M * p.r; i += kSkThreads) sXA[i] = p.xa[i];
-  ok = __all_sync(0xffffffffu, wait_bar(bar_b, 0, waiter)) && ok;
+  wait_bar(bar_b, 0, final_wt);
+  __syncwarp();
 
   // ---- 4. cluster barrier: every partial has landed in its owner's buffer; after
   // it no CTA touches another's shared memory, so each may finish and leave
@@ -311,6 +317,8 @@ __global__ void __launch_bounds__(256, F8 ? 6 : 1) qlora_xa_kernel(const __grid_
   uint64_t *bar = reinterpret_cast<uint64_t *>(sPart + kTokens * p.r);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(bar + 1);
   const Waiter waiter{abort_flag, p.limit_ns};
+  volatile int no_abort = 0;
+  const Waiter final_wt{&no_abort, drain_limit_ns(p.limit_ns)};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const uint32_t rank = cluster_ctarank();
@@ -354,9 +362,12 @@ __global__ void __launch_bounds__(256, F8 ? 6 : 1) qlora_xa_kernel(const __grid_
         dst[1] = hi;
       }
     }
-    const bool got = __syncthreads_and(wait_bar(bar, static_cast<uint32_t>(pass & 1), waiter)) != 0;
-    ok = ok && got;
-    if (!ok) break;
+    ok = __syncthreads_and(wait_bar(bar, static_cast<uint32_t>(pass & 1), waiter)) != 0;
+    if (!ok) {
+      // given up: the copies in flight land before the block may end (bounded)
+      if (tid == 0) wait_bar(bar, static_cast<uint32_t>(pass & 1), final_wt);
+      break;
+    }
     if (active) {
       for (int kst = my_part; kst < rows / 16; kst += nsplit) {
         const uint32_t x0 = smem_u32(sX + g * xpitch + kst * 16 + 2 * c);
