@@ -251,6 +251,8 @@ def linear_bwd(dY: torch.Tensor, X, XA: Optional[torch.Tensor], Wq: NF4Weight,
     if isinstance(X, FP8Tensor):
         return _linear_bwd_ckpt(dY, X, XA, Wq, A, B, s, need_dx, workspace, dX, dA, dB, keep_bits, dropout_p,
                                 accumulate)
+    if accumulate and (dA is None or dB is None):
+        raise ValueError("accumulate needs the dA and dB to add into")
     dY = _bf16_2d(dY, "dY")
     X = _bf16_2d(X, "X")
     A = _bf16_2d(A, "A")
@@ -265,8 +267,6 @@ def linear_bwd(dY: torch.Tensor, X, XA: Optional[torch.Tensor], Wq: NF4Weight,
         dA = torch.empty(Wq.cols, r, dtype=torch.float32, device=dev)
     if dB is None:
         dB = torch.empty(r, Wq.rows, dtype=torch.float32, device=dev)
-    if accumulate and (dA is None or dB is None):
-        raise ValueError("accumulate needs the dA and dB to add into")
     if workspace is None:
         workspace = make_workspace(M, Wq.rows, Wq.cols, r, dev, dropout=keep_bits is not None)
     st = Wq.c_struct()
