@@ -698,6 +698,7 @@ qlora_status fp8_bwd_impl(const uint16_t *dY, int64_t M, const qlora_fp8_t *X, c
       (dB && !aligned16(dB)) || (dX && !aligned16(dX)) || (XA && !aligned16(XA)) ||
       (workspace && !aligned16(workspace)))
     return QLORA_ERR_MISALIGNED;
+  if (dX && overlap_bf16(dX, M * K, dY, M * N)) return QLORA_ERR_INVALID_ARG;
   if (M * (N / 128) >= (1ll << 31)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   DeviceInfo *d = nullptr;
   if ((st = device_info(&d)) != QLORA_OK) return st;
@@ -745,7 +746,7 @@ qlora_status bwd_ckpt_impl(const uint16_t *dY, const qlora_fp8_t *X, const float
   if (!aligned16(dY) || !aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB) ||
       (dX && !aligned16(dX)) || (XA && !aligned16(XA)) || (workspace && !aligned16(workspace)))
     return QLORA_ERR_MISALIGNED;
-  if (!(s == s)) return QLORA_ERR_INVALID_ARG;
+  if (!(s == s) || (dX && overlap_bf16(dX, M * K, dY, M * N))) return QLORA_ERR_INVALID_ARG;
   if ((st = check_dropout(keep, drop_p)) != QLORA_OK) return st;
   DeviceInfo *d = nullptr;
   if ((st = device_info(&d)) != QLORA_OK) return st;

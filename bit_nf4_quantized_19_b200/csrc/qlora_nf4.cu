@@ -31,6 +31,13 @@ std::atomic<int> g_gemm_pairing{1};        // CTA-pair GEMM where the output wid
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether two bf16 tensors of na and nb values share memory.  A result over an operand of its GEMM is
+// refused: its tiles are written while others of the operand are still to be read.
+bool overlap_bf16(const void *a, int64_t na, const void *b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 2 * static_cast<uintptr_t>(nb) && y < x + 2 * static_cast<uintptr_t>(na);
+}
+
 qlora_status cuda_status(cudaError_t e) { return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA; }
 
 constexpr int kSkSmemLimit = 200 * 1024;
@@ -855,7 +862,7 @@ qlora_status linear_fwd_impl(const uint16_t *X, int64_t M, const qlora_nf4_t *Wq
   if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(Y) ||
       (XA_out && !aligned16(XA_out)) || (workspace && !aligned16(workspace)))
     return QLORA_ERR_MISALIGNED;
-  if (!(s == s)) return QLORA_ERR_INVALID_ARG;
+  if (!(s == s) || overlap_bf16(Y, M * Wq->rows, X, M * Wq->cols)) return QLORA_ERR_INVALID_ARG;
   if ((st = check_dropout(keep, drop_p)) != QLORA_OK) return st;
   DeviceInfo *d = nullptr;
   if ((st = device_info(&d)) != QLORA_OK) return st;
@@ -907,6 +914,8 @@ qlora_status linear_bwd_impl(const uint16_t *dY, const uint16_t *X, const float 
       (workspace && !aligned16(workspace)))
     return QLORA_ERR_MISALIGNED;
   if (!(s == s)) return QLORA_ERR_INVALID_ARG;
+  if (dX && (overlap_bf16(dX, M * Wq->cols, dY, M * Wq->rows) || overlap_bf16(dX, M * Wq->cols, X, M * Wq->cols)))
+    return QLORA_ERR_INVALID_ARG;
   if ((st = check_dropout(keep, drop_p)) != QLORA_OK) return st;
   DeviceInfo *d = nullptr;
   if ((st = device_info(&d)) != QLORA_OK) return st;

@@ -18,6 +18,8 @@
  *     The library never allocates or frees memory; scratch space is passed in
  *     explicitly as `workspace` (size from qlora_linear_workspace_bytes).
  *   - Every pointer must be 16-byte aligned (QLORA_ERR_MISALIGNED otherwise).
+ *   - Outputs share no memory with inputs or with one another.  Y over X, or dX over dY or a
+ *     bf16 X, is refused (QLORA_ERR_INVALID_ARG).
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy default
  *     stream).  Argument, shape and alignment errors are reported synchronously
  *     before anything is launched; launch failures map to QLORA_ERR_CUDA.
@@ -46,7 +48,8 @@ typedef struct CUstream_st *qlora_stream_t;
 
 typedef enum {
   QLORA_OK = 0,
-  QLORA_ERR_INVALID_ARG = 1,       /* null pointer, bad size, r out of range      */
+  QLORA_ERR_INVALID_ARG = 1,       /* null pointer, bad size, r out of range, a    */
+                                   /* result over its operand                      */
   QLORA_ERR_MISALIGNED = 2,        /* a pointer is not 16-byte aligned            */
   QLORA_ERR_UNSUPPORTED_SHAPE = 3, /* shape the fused GEMM does not cover         */
   QLORA_ERR_CUDA = 4,              /* a CUDA runtime/driver call failed            */
