@@ -574,7 +574,6 @@ qlora_status launch_skinny8(const qlora_fp8_t &X, const qlora_fp8_t &W, const ui
   if (r && !make_map_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, B, N, r, 2 * N, R, r, CU_TENSOR_MAP_SWIZZLE_NONE))
     return QLORA_ERR_CUDA;
   Skinny8Params p{};
-  p.x = X.codes;
   p.xs = X.scales;
   p.ws = W.scales;
   p.pitch = pitch;

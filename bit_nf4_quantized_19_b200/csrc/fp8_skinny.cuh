@@ -43,7 +43,6 @@ constexpr int kS8MaxCluster = 8;
 constexpr int kS8MaxXaParts = 8;
 
 struct Skinny8Params {
-  const uint8_t *x;        // codes [M, K]
   const uint8_t *xs;       // factors [M, pitch]
   const uint8_t *ws;       // factors [N / 128, pitch]
   int pitch;

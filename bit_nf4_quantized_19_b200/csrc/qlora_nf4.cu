@@ -696,7 +696,6 @@ qlora_status launch_skinny(const uint16_t *X, int64_t M, const qlora_nf4_t *Wq, 
   p.codes = Wq->codes;
   p.q8 = Wq->q8;
   p.step = Wq->step;
-  p.B = B;
   p.xa = xa;
   p.Y = Y;
   p.M = static_cast<int>(M);

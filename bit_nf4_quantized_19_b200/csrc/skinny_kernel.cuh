@@ -49,7 +49,6 @@ struct SkinnyParams {
   const uint8_t *codes;   // packed NF4 of W [N, K]
   const uint8_t *q8;      // null: single-level constants, step[block] = the block absmax
   const float *step;
-  const uint16_t *B;      // [r, N] bf16
   const float *xa;        // [M, r] fp32, written by qlora_xa_kernel
   uint16_t *Y;            // [M, N] bf16
   int M, K, N, r;
