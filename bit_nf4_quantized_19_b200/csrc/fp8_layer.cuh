@@ -616,11 +616,16 @@ size_t fp8_hl_bytes(int64_t M, int r) { return align256(static_cast<size_t>(M) *
 size_t fp8_terms_bytes(int64_t M, int r) { return align256(static_cast<size_t>(M) * 3 * nn_proj(r) * 2 + 128); }
 
 // The calls of the few-token kernel.  Each of its CTAs adds the parts of XA, M r values, and takes the
-// rank-r product of its rows without the tensor core, so with more the GEMM is faster: 8192 x
-// 8192, r 64, 4 tokens 16.9 us (18.1 on the GEMM), 6 tokens 18.0 (18.0), 8 tokens 18.7 (18.1).  The
-// launch has a row of clusters for each 128 weight rows, at most 65535.
+// rank-r product of its rows without the tensor core; the GEMM's form pays two more launches and,
+// past rank 64, a second pass for XA.  Both forced on 6 layers (4096 x 4096 to 8192 x 22016), ranks 8 to
+// 128, 1 to 8 tokens, replayed, us:
+//   8192 x 8192   1 token, r 16: 16.2 (GEMM 17.9); 8 tokens, r 64: 18.6 (18.5); 8 tokens, r 128: 23.0 (26.6)
+//   11008 x 4096  1 token, r 16: 13.9 (14.6); 8 tokens, r 64: 17.2 (14.8); 8 tokens, r 128: 19.7 (21.3)
+//   4096 x 11008  1 token, r 16: 12.4 (15.0); 8 tokens, r 64: 17.4 (15.5); 8 tokens, r 128: 18.9 (24.8)
+// This rule takes the faster form, or one within 2% of it, in 232 of the 252 calls, and one at most 10%
+// slower in the others.  The launch has a row of clusters for each 128 weight rows, at most 65535.
 bool fp8_few_tokens(int64_t M, int64_t N, int r) {
-  return M <= kS8MaxTokens && M * r <= 384 && N / kS8Rows <= 65535;
+  return M <= kS8MaxTokens && (M * r <= 384 || r > kAmPass) && N / kS8Rows <= 65535;
 }
 
 size_t fp8_fwd_workspace(int64_t M, int64_t N, int64_t K, int r, const GemmUnits &u) {

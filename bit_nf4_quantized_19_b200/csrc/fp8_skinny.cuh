@@ -1,4 +1,4 @@
-// Few-token forward (M <= 8, M r <= 384) of the linear layer on an 8-bit base:
+// Few-token forward (M <= 8; fp8_few_tokens says for which ranks) of the linear layer on an 8-bit base:
 //     Y = deq(X) deq(W)^T + s (XA) B
 // Bound by reading the 8-bit weight once, so the design keeps the weight stream deep and
 // everything else beside it.  XA comes from qlora_xa_kernel<true> (clusters of eight

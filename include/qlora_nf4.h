@@ -330,7 +330,8 @@ size_t qlora_fp8_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);
  * accumulated in fp32.  r = 0 with A = B = XA_out = NULL: the product alone.  X is all
  * the backward needs of the input: it is the 8-bit activation checkpoint.
  * N % 128 == 0, K % 128 == 0, r a multiple of 8 in [8, 128] (or 0).  Few tokens (M <= 8
- * with M r <= 384, and M <= 128) take forms of their own, bound by reading W.  Ordering and graph capture as qlora_linear_fwd.
+ * with M r <= 384 or r > 64, and M <= 128) take forms of their own, bound by reading W.
+ * Ordering and graph capture as qlora_linear_fwd.
  */
 qlora_status qlora_fp8_linear_fwd(const qlora_fp8_t *X, const qlora_fp8_t *W, const uint16_t *A,
                                   const uint16_t *B, int r, float s, uint16_t *Y, float *XA_out,

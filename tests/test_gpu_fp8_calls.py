@@ -293,3 +293,23 @@ def test_calls_that_read_what_the_call_before_wrote(q, M, r):
     torch.cuda.synchronize()
     assert q.device_status() == (0, 0)
     assert all(same(g, want[i]) for i, g in got)
+
+
+# ------------------------------------------------------------------ which form a forward takes
+@pytest.mark.parametrize("M,r,few", [(1, 0, True), (8, 48, True), (8, 64, False), (6, 64, True), (8, 72, True), (8, 128, True),
+                                     (3, 128, True), (9, 0, False), (9, 128, False)])
+def test_few_token_form_by_tokens_and_rank(q, M, r, few):
+    """Up to 8 tokens: the few-token kernel while M r <= 384, and for every rank past 64, where the GEMM's
+    form needs two passes for XA."""
+    import torch
+    p = Problem(M, 256, 384, r)
+    Xq, Wq = q.fp8_quantize(dev(p.X)), q.fp8_quantize_weight(dev(p.W))
+    ad = (dev(p.A), dev(p.B), p.s) if r else ()
+    q.profile_enable(True)
+    try:
+        q.fp8_linear_fwd(Xq, Wq, *ad)
+        torch.cuda.synchronize()
+        kinds = [k for k, _ in q.profile_read()[0]]
+    finally:
+        q.profile_enable(False)
+    assert ("fp8_skinny" in kinds) == few and ("fp8_gemm_fwd" in kinds) == (not few)
