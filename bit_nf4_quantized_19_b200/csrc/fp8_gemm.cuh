@@ -522,9 +522,20 @@ __global__ void __launch_bounds__(256) fp8_reduce_kernel(const float *part, int 
   pdl_trigger();
   pdl_wait();
   if (i >= total) return;
-  float4 v = ld_global_f4(part + i);
-  for (int s = 1; s < splits; ++s) {
-    const float4 f = ld_global_f4(part + s * total + i);
+  // two parts' loads before their adds: one at a time takes 0.3 us more of 8 (9 tokens, 4096 x 4096);
+  // eight need registers past 32, and its CTAs no longer start beside the GEMM's (128 tokens of
+  // 22016 x 8192: 46 us, 44)
+  const float *src = part + i;
+  float4 v = ld_global_f4(src);
+  int s = 1;
+#pragma unroll 1
+  for (; s + 1 < splits; s += 2) {
+    const float4 f = ld_global_f4(src + s * total), g = ld_global_f4(src + (s + 1) * total);
+    v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
+    v.x += g.x; v.y += g.y; v.z += g.z; v.w += g.w;
+  }
+  if (s < splits) {
+    const float4 f = ld_global_f4(src + s * total);
     v.x += f.x; v.y += f.y; v.z += f.z; v.w += f.w;
   }
   *reinterpret_cast<uint2 *>(out + i) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
