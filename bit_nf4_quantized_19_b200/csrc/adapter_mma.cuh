@@ -25,7 +25,7 @@
 //               row's power of two, dropped-out elements zeroed;
 //               G with QUANT: two groups take a pair, the other two the next, two lanes a row,
 //               whose 128 values are one block: amax, factor byte and codes.
-// Stages of 64 rather than 128 halve what a slot holds (24 to 40 KB): a slot's Q load, conversion
+// Stages of 64 rather than 128 halve what a slot holds (G 18 to 24 KB, XA 24, gradients 24 to 40): a slot's Q load, conversion
 // and MMAs follow one another, so the number of slots sets how much of that latency is
 // hidden.
 // The activation is the MMA's A operand: K-major for projections (128 rows of 64 values),
@@ -34,9 +34,12 @@
 // bf16 terms side by side [M, 3 w], whose sum carries all 24 bits; the drain adds the
 // three column ranges.  A launch computes up to 64 columns (32 sums per drain thread);
 // wider adapters take two.
-// Measured (8192 x 8192, r 64): XA 40 us, dA 43 (67 MB each: the path of a stage through conversion,
-// MMAs and barriers, about 1500 cycles for 128 values of the 700 that HBM allows), G with the
-// quantization 52 (201 MB), dB 38 (134 MB, 3.5 TB/s of a launch that starts and ends in 8 us).
+// Measured (8192 x 8192, r 64, events around each launch): XA 38 us, dA 45 (67 MB each: the path of a
+// stage through conversion, MMAs and barriers, about 1500 cycles for 128 values of the 700 that HBM
+// allows), G with the quantization 43 (201 MB, 4.6 TB/s), dB 38 (134 MB, 3.5 TB/s).  Start, cluster skew
+// and reduction are 7 to 11 us of each, and the clusters of few row tiles leave SMs idle: 64 row
+// tiles in two parts are 128 CTAs for 148 SMs, dB of 11008 columns 86.  r 128 takes two launches
+// of each: forward 440 us (402 at r 64), backward 577 (468).
 // Ring slots of two stages, for one wait and commit per 128 values, changed nothing.
 #pragma once
 #include "common.cuh"

@@ -24,8 +24,8 @@
 // MMA's rows and the tokens, rounded up to 32, its columns, so the tensor core takes nt / 256 of
 // the time and HBM is the bound; the smaller stage (16 KB of weight, at most 8 KB of tokens) makes
 // eight of them.  The epilogue's lanes are outputs: it stores a token's 32 of them at once, no
-// staging.  13 tokens of 8192 x 22016, replayed: 35 us, 40 as 256 token rows; 22016 x 8192: 36
-// and 53 (floor 28).
+// staging.  13 tokens, no adapter, weights in turn, replayed: 8192 x 22016 35 us (40 as 256 token
+// rows), 22016 x 8192 35 (54), floor 28; with r 64 and so XA in front 38 (43) and 39 (60).
 //
 // TMEM: two 256-column accumulators that overlap by 32 columns, [0, 256) and [224, 480),
 // leave 32 columns for two factor slots.  The epilogue drains the shared columns of a
@@ -37,12 +37,14 @@
 //   1     TMEM allocator; in the leader the MMA issuer
 //   4..7  epilogue: TMEM -> bf16 (or fp32 partials) -> shared memory -> TMA store
 //   8..11 factor writers: each TMEM lane quadrant needs its own copy of the factor tile
-// Measured (SM clock near 1.9 GHz): forward of 8192 tokens, 22016 x 8192, r 64: 0.98 to 1.02 ms,
-// 2.9 to 3.0 PFLOP/s, where twice the measured bf16 rate is 3.39; dX of 8192 tokens, 8192 x 8192:
-// 345 us, 3.2.  The tensor pipe is active 90% of the SMs' cycles; the rest is the switch between
-// tiles (about 1500 cycles) and, with few tiles, the last round: 4096 x 4096 x 4096 is 3.46
-// rounds, 54 us for 41.  Dividing a last round's tiles as well cost more in its exchange than
-// the half round (70 us).
+// Measured: forward of 8192 tokens, 22016 x 8192, r 64: one launch takes 1.455 M cycles, 1.03 ms alone
+// (2.9 PFLOP/s, where twice the measured bf16 rate is 3.39) and 1.17 ms under a continuous load.  The
+// tensor pipe is active 89% of them, 96% of the cycles in which the SMs are: the power limit bounds
+// it, with the SM clock at 1.41 GHz and 1.24 GHz.  dX of 8192 tokens, 8192 x 8192: 345 to 362 us.
+// The rest is the switch between tiles (about 1500 cycles), start and end, and, with few tiles, the
+// last round: 1024 tokens of 18944 x 8192, four whole rounds: active 84%; 4096 x 4096 x 4096,
+// 3.46 rounds: 60 us for 41.  Dividing a last round's tiles as well cost more in its exchange than
+// the half round (57 to 70 us).
 #pragma once
 #include "common.cuh"
 #include "fp8_quant.cuh"

@@ -17,7 +17,7 @@
 //     word w, codes 0, 1 and 2, 3 the fragment's two halves, for W and X alike.
 //   - The CTAs of XA fit beside two of these on an SM (72 and 40 registers, small chunks), so the
 //     weight pass has its places from the start: with XA on SMs of its own, whole clusters
-//     waited for it (1 token, r 64, N 8192, K 22016, replayed: 40 us, now 32.5; the weight
+//     waited for it (1 token, r 64, N 8192, K 22016, replayed: 40 us, now 34; the weight
 //     alone at 6.45 TB/s is 28).
 //   - X's codes come by TMA too, and two warps, on alternate blocks, convert them for all: they
 //     stage each block's f16 fragments, in the order the product warps' registers take them,

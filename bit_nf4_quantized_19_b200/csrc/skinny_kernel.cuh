@@ -273,10 +273,11 @@ __global__ void __launch_bounds__(kSkThreads, 3) qlora_skinny_kernel(
   }
 }
 
-// XA = X A for few tokens: one cluster of kXaCluster CTAs, rank q takes rows
-// [q kx, (q+1) kx) of the contraction in chunks of `chunk` rows, each chunk of A
-// (contiguous) and of every token row of X fetched by one bulk copy; X rows on
-// the MMA's M (tokens), adapter columns on N.  Partials are summed in rank order.
+// XA = X A for few tokens: clusters of kXaCluster CTAs (one for bf16 X), CTA `slice` of them all
+// takes rows [slice kx, (slice + 1) kx) of the contraction in chunks of `chunk` rows, each chunk of
+// A (contiguous) and of every token row of a bf16 X fetched by one bulk copy; X rows on the MMA's M
+// (tokens), adapter columns on N.  A cluster's partials are summed in rank order into its own
+// [M, r]; whoever reads several adds them.
 constexpr int kXaCluster = 8;
 
 struct XaParams {
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(256, F8 ? 6 : 1) qlora_xa_kernel(const __grid_
       p.xa[static_cast<int>(blockIdx.y) * p.M * p.r + i] = __fmul_rn(v, p.scale);
     }
   }
-  cluster_sync_all();   // the peers' partials stay until rank 0 has read them
+  cluster_sync_all();   // a CTA's partials stay until rank 0 (of 8-bit X, every rank) has read them
 }
 
 // Shared-memory plan of one launch; false when nothing fits in `limit` bytes.
