@@ -81,7 +81,9 @@ QDEV bool wait_bar(uint64_t *bar, uint32_t parity, const Waiter &w) {
 
 // Limit of the waits for what is already in flight (copies, MMAs) before a block gives up
 // its shared memory and TMEM: long enough whatever the caller's limit is.
-QDEV uint64_t drain_limit_ns(uint64_t limit_ns) { return limit_ns > 50000000ull ? limit_ns : 50000000ull; }
+__host__ __device__ __forceinline__ uint64_t drain_limit_ns(uint64_t limit_ns) {
+  return limit_ns > 50000000ull ? limit_ns : 50000000ull;
+}
 
 // ------------------------------------------------------------------ global flags
 QDEV uint32_t ld_acquire_u32(const unsigned int *a) {

@@ -126,6 +126,7 @@ struct GemmParams {
   const uint16_t *lora_w;  // fwd: B [r, N];  dX: A [K, r]
   uint16_t *out;     // Y [M, N] or dX [M, K]
   uint64_t limit_ns;
+  uint64_t drain_ns; // drain_limit_ns(limit_ns)
   int split_base;    // first tile of the split last round (a multiple of the unit count)
   int split_count;   // tiles split into two contraction halves (0: no split)
   int kb_mid;        // first main stage of the second half
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       // peer's own copy of that stage has landed, or not at all after an abort: the
       // wait is bounded either way, and this CTA's copies have landed when it ends.
       volatile int no_abort = 0;
-      const Waiter final_wt{&no_abort, drain_limit_ns(p.limit_ns)};
+      const Waiter final_wt{&no_abort, p.drain_ns};
       for (int s = 0; s < kStages; ++s)
         if (armedB & (1u << s)) wait_bar(&full_B[s], (lastB >> s) & 1u, final_wt);
     }
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     if (lane == 0) {
       volatile int no_abort = 0;
-      const Waiter final_wt{&no_abort, drain_limit_ns(p.limit_ns)};
+      const Waiter final_wt{&no_abort, p.drain_ns};
       for (int s = 0; s < kStagesW; ++s)
         if (armedW & (1u << s)) wait_bar(&full_W[s], (lastW >> s) & 1u, final_wt);
     }
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       // released (bounded).
       commit(drain);
       volatile int no_abort = 0;
-      const Waiter final_wt{&no_abort, drain_limit_ns(p.limit_ns)};
+      const Waiter final_wt{&no_abort, p.drain_ns};
       wait_bar(drain, 0, final_wt);
     }
   } else if (warp == 1) {
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       // the leader's MMAs read this CTA's shared memory and write its TMEM: they
       // complete before either is released (bounded)
       volatile int no_abort = 0;
-      const Waiter final_wt{&no_abort, drain_limit_ns(p.limit_ns)};
+      const Waiter final_wt{&no_abort, p.drain_ns};
       wait_bar(drain, 0, final_wt);
     }
   } else if (warp >= 4 && warp < 8) {

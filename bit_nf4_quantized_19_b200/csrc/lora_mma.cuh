@@ -51,6 +51,7 @@ struct LoraMmaParams {
   int ldT;
   int layout;
   uint64_t limit_ns;
+  uint64_t drain_ns;   // drain_limit_ns(limit_ns)
   // A second gradient product in the same launch: row tiles [tiles0, gridDim.x) compute
   // it from the second pair of tensor maps.  It shares the contraction, nn and the
   // splits; it has its own rows, output and layout.  tiles0 = gridDim.x: none.
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kLmThreads, 1)
       if (++s == S) { s = 0; ph ^= 1u; }
     }
     volatile int no_abort = 0;
-    const Waiter fw{&no_abort, drain_limit_ns(p.limit_ns)};
+    const Waiter fw{&no_abort, p.drain_ns};
     for (int k = 0; k < S; ++k)
       if (armed & (1u << k)) wait_bar(&full[k], (last >> k) & 1u, fw);
   } else if (warp == 1 && lane == 0) {
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(kLmThreads, 1)
     const int q = warp & 3;
     const int rl = q * 32 + lane;
     volatile int no_abort = 0;
-    const Waiter dw{&no_abort, drain_limit_ns(p.limit_ns)};
+    const Waiter dw{&no_abort, p.drain_ns};
     const bool got = __all_sync(0xffffffffu, wait_bar(done, 0, dw) ? 1 : 0);
     tc_fence_after();
     const int pitch = lm_partial_pitch(p.nn);

@@ -42,6 +42,7 @@ struct MergeParams {
   float s;
   float levels[16];
   uint64_t limit_ns;
+  uint64_t drain_ns;   // drain_limit_ns(limit_ns)
 };
 
 // Shared memory: the operand stages, then (bf16 base) the base tile that becomes the
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
     }
     // no copy may still be in flight when the block exits
     volatile int no_abort = 0;
-    const Waiter fw{&no_abort, drain_limit_ns(p.limit_ns)};
+    const Waiter fw{&no_abort, p.drain_ns};
     for (int st = 0; st < p.stages; ++st) wait_bar(&full[st], 0, fw);
     wait_bar(base_full, 0, fw);
   } else if (warp == 1 && lane == 0) {
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
 #pragma unroll
     for (int i = 0; i < 16; ++i) L[i] = p.levels[i];
     volatile int no_abort = 0;
-    const Waiter dw{&no_abort, drain_limit_ns(p.limit_ns)};
+    const Waiter dw{&no_abort, p.drain_ns};
     const bool got = __all_sync(0xffffffffu, (wait_bar(done, 0, dw) && wait_bar(base_full, 0, dw)) ? 1 : 0) &&
                      *abort_flag == 0;
     tc_fence_after();

@@ -493,6 +493,7 @@ qlora_status launch_lora_mma(const LmOperands &o, int64_t contraction, int nn, L
   p.tmem_cols = g.tmem_cols;
   p.splits = g.splits;
   p.limit_ns = static_cast<uint64_t>(g_wait_limit_us.load()) * 1000ull;
+  p.drain_ns = drain_limit_ns(p.limit_ns);
   const int smem = lora_mma_smem_bytes(nn, g.num_stages, g.sub);
   if (smem > kLmSmemMax) return QLORA_ERR_UNSUPPORTED_SHAPE;
   cudaLaunchConfig_t cfg{};
@@ -804,6 +805,7 @@ qlora_status launch_gemm(const uint16_t *act, int64_t M, const qlora_nf4_t *Wq,
   p.lora_w = lora_w;
   p.out = out;
   p.limit_ns = static_cast<uint64_t>(g_wait_limit_us.load()) * 1000ull;
+  p.drain_ns = drain_limit_ns(p.limit_ns);
   const Nf4Tables &T = nf4_tables();
   std::memcpy(p.levels, T.levels, sizeof(p.levels));
   const int tiles = p.num_m_tiles * p.num_w_tiles;
@@ -1141,6 +1143,7 @@ qlora_status qlora_nf4_merge(const qlora_nf4_t *Wq, const uint16_t *W16, int64_t
   p.stages = (r + 63) / 64;
   p.s = s;
   p.limit_ns = static_cast<uint64_t>(g_wait_limit_us.load()) * 1000ull;
+  p.drain_ns = drain_limit_ns(p.limit_ns);
   std::memcpy(p.levels, nf4_tables().levels, sizeof(p.levels));
   CUtensorMap tm_bt, tm_a, tm_base, tm_out;
   // B [r, N]: x = n (inner), y = j; A [K, r]: x = j (inner), y = k.  Boxes reach j = 64 per

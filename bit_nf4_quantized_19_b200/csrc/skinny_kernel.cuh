@@ -224,11 +224,6 @@ __global__ void __launch_bounds__(kSkThreads, 3) qlora_skinny_kernel(
     }
   }
 
-  volatile int no_abort = 0;
-  const Waiter final_wt{&no_abort, drain_limit_ns(p.limit_ns)};
-  // given up: the boxes in flight land before the block may end (bounded)
-  for (int mb = 0; !ok && mb < nmb; ++mb) wait_bar(&bars[mb], 0, final_wt);
-
   // ---- 3. push the partial Y rows to the rank that finishes them: slot
   // [this rank][row within the owner's R][token] of the owner's receive buffer
   {
@@ -254,7 +249,14 @@ __global__ void __launch_bounds__(kSkThreads, 3) qlora_skinny_kernel(
   // XA comes from the XA kernel: wait for that grid (a no-op when launched plainly)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i = tid; i < p.M * p.r; i += kSkThreads) sXA[i] = p.xa[i];
-  wait_bar(bar_b, 0, final_wt);
+  if (!__all_sync(0xffffffffu, wait_bar(bar_b, 0, waiter) && ok)) {
+    // given up: the copies in flight land before the block may end (bounded)
+    volatile int no_abort = 0;
+    const Waiter final_wt{&no_abort, drain_limit_ns(p.limit_ns)};
+#pragma unroll 1
+    for (int i = 0; i < nmb; ++i) wait_bar(&bars[i], 0, final_wt);
+    wait_bar(bar_b, 0, final_wt);
+  }
   __syncwarp();
 
   // ---- 4. cluster barrier: every partial has landed in its owner's buffer; after

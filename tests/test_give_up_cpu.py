@@ -35,7 +35,14 @@ def test_the_kernels_are_found():
 @pytest.mark.parametrize("name,text", kernels(), ids=[n for n, _ in kernels()])
 def test_the_last_waits_have_their_own_limit(name, text):
     limits = FINAL.findall(text)
-    assert limits and all(x.startswith("drain_limit_ns(") for x in limits)
+    assert limits and all(x == "p.drain_ns" or x.startswith("drain_limit_ns(") for x in limits)
+
+
+def test_limits_from_the_host():
+    """Each struct with a drain_ns is filled from drain_limit_ns by its one launch."""
+    structs = sum(len(re.findall(r"uint64_t drain_ns;", open(os.path.join(build.CSRC, n)).read())) for n in build.HEADERS)
+    host = open(os.path.join(build.CSRC, "qlora_nf4.cu")).read()
+    assert structs == len(re.findall(r"p\.limit_ns = [^\n]*\n  p\.drain_ns = drain_limit_ns\(p\.limit_ns\);", host)) == 3
 
 
 @pytest.mark.parametrize("name,text", [k for k in kernels() if "mma_commit" in k[1]],
