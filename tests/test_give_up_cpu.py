@@ -35,7 +35,10 @@ def test_the_kernels_are_found():
 @pytest.mark.parametrize("name,text", kernels(), ids=[n for n, _ in kernels()])
 def test_the_last_waits_have_their_own_limit(name, text):
     limits = FINAL.findall(text)
-    assert limits and all(x == "p.drain_ns" or x.startswith("drain_limit_ns(") for x in limits)
+    if not limits:      # no phase to wait on, or no registers for it: a fixed delay, long against a copy's time
+        assert re.search(r"if \(!ok\) \{\s*(#pragma unroll 1\s*)?for \(int i = 0; i < 200; \+\+i\) __nanosleep\(1000\);", text)
+        return
+    assert all(x == "p.drain_ns" or x.startswith("drain_limit_ns(") for x in limits)
 
 
 def test_limits_from_the_host():
